@@ -421,8 +421,8 @@ rxl_status rxl_layernorm_bwd(const rxl_norm_desc *desc, const void *dy, long lon
  * they add nothing to the entropy. A row with nothing but -inf has lse -inf,
  * logp and top_logp -inf, entropy 0. A row with +inf or NaN in it has NaN
  * for logp, entropy and top_logp (lse: +inf or NaN) and ids in [0, V).
- * Sums are float32, relative to the running maximum. So are logp and
- * top_logp: logits that are all far from zero cost lse places, but not them.
+ * Sums are float32, relative to the running maximum. So are logp, top_logp and
+ * entropy: logits that are all far from zero cost lse places, but not them.
  */
 typedef struct {
   long long rows;
