@@ -355,10 +355,13 @@ rxl_status rxl_mem_update_rings(rxl_ring *const *rings, const void *const *srcs,
  *   y    = (s - mean) rstd gamma + beta
  *   rows   rows of D elements; 0 <= rows <= 2^40
  *   D      row length, 1 <= D <= 16384 (beyond: RXL_ERR_UNSUPPORTED)
- *   eps    >= 0 and finite. A row of equal elements with eps == 0 gives NaN.
+ *   eps    >= 0 and finite. A row of equal elements with eps == 0 has no
+ *          result: NaN, or what rounding leaves of 0 / 0.
  * x, residual, y, sum [rows, D] and gamma, beta [D] of desc.dtype; mean, rstd
  * [rows] float32. Statistics and sums are float32 whatever the type, from
- * two passes over the row on chip.
+ * two passes over the row on chip; a row whose mean is more than 16 times
+ * sqrt(variance + eps) is centred a second time, by the mean of what the first
+ * one left (equal elements of any size give y = beta).
  *   residual  nullable. sum (nullable, only with a residual) receives s.
  *   mean, rstd  nullable together; what rxl_layernorm_bwd takes.
  * y may be x or residual, and sum may be the other one or (without being y)

@@ -2,20 +2,21 @@
 // reduction of the weights' gradients (include/rxl.h: rxl_layernorm_*).
 //
 // Memory-bound: a row is read once, held in registers, and written once. A
-// group of G threads takes a row, E elements a thread, so both sweeps over
-// the row that the statistics take (sum, then squared differences) and the
-// output run on registers; a group is a few lanes or a warp (shuffles) or
-// several warps (a named barrier around a few words of shared memory). Groups
-// are mostly persistent: they keep their columns of gamma and beta, and the
-// next row's loads are in flight while a row is worked on.
+// group of G threads takes a row, E elements a thread, so the sweeps over the
+// row that the statistics take (sum, then squared differences; two more where
+// the mean is far larger than the spread) and the output run on registers; a
+// group is a few lanes or a warp (shuffles) or several warps (a named barrier
+// around a few words of shared memory). Groups are mostly persistent: they keep
+// their columns of gamma and beta, and the next row's loads are in flight while
+// a row is worked on.
 //
 // The backward keeps, for its columns, running sums of dy xh and dy over its
 // rows: dgamma and dbeta cost no second reading of dy and s. A block joins
 // its groups' sums in shared memory and writes one partial row; a second
 // kernel adds the partial rows in block order, so results do not depend on
-// timing (of few rows one block writes the result). The sums leave few registers, so rows come by asynchronous copies
-// into each thread's own words of shared memory, three rows deep, and are
-// read from there for both sweeps.
+// timing (of few rows one block writes the result). The sums leave few
+// registers, so rows come by asynchronous copies into each thread's own words
+// of shared memory, three rows deep, and are read from there for both sweeps.
 //
 // Measured (the card copies at 6.78 TB/s): forward with residual, bf16, 8192 x
 // 1024 12.4 us (5.4 TB/s: five turns of 1824 rows, the last half empty), 32768 x
@@ -252,19 +253,63 @@ norm_fwd_kernel(const T *x, long long xs, const T *res, long long rs, const T *g
     }
     float a[1] = {both(acc)};
     R::sum(a, shared, slot);
-    const float mu = a[0] * inv_d;
+    float mu = a[0] * inv_d;
     if (RES && sum)
 #pragma unroll
       for (int i = 0; i < R::kN; ++i) R::write(sum + row * ss, D, i, s);
-    acc = Pair(0.f, 0.f);
-    const Pair neg(-mu, -mu);
+    // Takes `off` from the row; a[0]: the sum of the squares that are left.
+    const auto centre = [&](float off) {
+      acc = Pair(0.f, 0.f);
+      const Pair neg(-off, -off);
 #pragma unroll
-    for (int p = 0; p < R::kP; ++p) {
-      s[p] = R::inside(add(s[p], neg), p, width);
-      acc = fma(s[p], s[p], acc);
+      for (int p = 0; p < R::kP; ++p) {
+        s[p] = R::inside(add(s[p], neg), p, width);
+        acc = fma(s[p], s[p], acc);
+      }
+      a[0] = both(acc);
+      R::sum(a, shared, slot);
+    };
+    // What rounding left of the mean is the differences' own mean. It counts
+    // only where the mean is far larger than the spread (1000.1 everywhere: y
+    // off by 0.02): such rows are centred once more. A warp's other rows by 0.
+    const auto far = [&]() { return mu * mu > 256.f * (a[0] * inv_d + eps); };
+    const auto any_far = [&]() { return G < 32 ? __any_sync(0xffffffffu, far()) : far(); };
+    const auto rest = [&]() {
+      acc = Pair(0.f, 0.f);
+#pragma unroll
+      for (int p = 0; p < R::kP; ++p) acc = add(acc, s[p]);
+      float r[1] = {both(acc)};
+      R::sum(r, shared, slot);
+      return far() ? r[0] * inv_d : 0.f;
+    };
+    // How the rare case is written decides what the usual one costs, whose
+    // registers are few (us without it, with it as a loop, and as a branch that
+    // centres again or that takes D c^2 from the squares: with residual 32768 x
+    // 4096 bf16 162, 162, 166, 166; without 65536 x 1024 42.4, 44.6, 43.6, 42.8;
+    // 32768 x 4096 85.0, 86.7, 85.7, 88.8; 4500 x 16384 f32 94, 95, 102, 105).
+    if constexpr (RES || !AHEAD) {
+      float off = mu;
+#pragma unroll 1
+      for (bool first_time = true;; first_time = false) {
+        centre(off);
+        if (!first_time || !any_far()) break;
+        off = rest();
+        mu += off;
+      }
+    } else {
+      centre(mu);
+      if (any_far()) {
+        const float c = rest();
+        mu += c;
+        if constexpr (G > 32) {
+          centre(c);
+        } else {
+          a[0] = max_nan(fmaf(-c * width, c, a[0]), 0.f);
+#pragma unroll
+          for (int p = 0; p < R::kP; ++p) s[p] = add(s[p], Pair(-c, -c));
+        }
+      }
     }
-    a[0] = both(acc);
-    R::sum(a, shared, slot);
     const float inv = 1.f / sqrtf(a[0] * inv_d + eps);
     if (!AHEAD) {
       R::read(gm, gamma, width);
