@@ -384,14 +384,36 @@ def make_adamw_desc(param_dtype=RXL_DTYPE_BF16, grad_dtype=RXL_DTYPE_BF16, state
     return rxl_adamw_desc(param_dtype, grad_dtype, state_bits, beta1, beta2, eps)
 
 
+def _check_adamw_sizes(t):
+    """ValueError unless the tensors of one entry hold its n elements in one
+    order. The list is made once, so this costs a step nothing."""
+    n = t["n"]
+    held = {k: t.get(k) for k in ("param", "master", "grad", "m", "v", "m_scale", "v_scale")}
+    held = {k: x for k, x in held.items() if x is not None and not isinstance(x, int)}
+    for k, x in held.items():
+        need = -(-n // 128) if k.endswith("_scale") else n
+        if x.numel() < need:
+            raise ValueError(f"{k} has {x.numel()} elements where {need} are read")
+    full = [x for k, x in held.items() if not k.endswith("_scale")]
+    alike = all(x.shape == full[0].shape and x.stride() == full[0].stride() for x in full)
+    for k, x in held.items():
+        # without gaps: the last element lies numel - 1 places behind the first
+        dense = sum((s - 1) * d for s, d in zip(x.shape, x.stride())) == x.numel() - 1
+        if n > 0 and not x.is_contiguous() and not (alike and dense and not k.endswith("_scale")):
+            raise ValueError(f"{k} is not contiguous (nor without gaps and in one order with the entry's other tensors)")
+
+
 def make_adamw_tensors(desc, tensors):
     """The list rxl_adamw_step takes, from dicts with the fields of
     rxl_adamw_tensor (master, m_scale, v_scale and weight_decay may be left
-    out). It holds addresses only: keep it with the tensors, for as long as
-    they stay where they are."""
+    out). An entry's tensors hold n elements or more (scales one for every
+    128), contiguous, or all in one other order without gaps (ValueError). The
+    list holds addresses only: keep it with the tensors, for as long as they
+    stay where they are."""
     out, d = (rxl_adamw_tensor * max(len(tensors), 1))(), _current_device()
     state = None if desc.state_bits == 8 else "f32"
     for i, t in enumerate(tensors):
+        _check_adamw_sizes(t)
         m, v = t.get("m"), t.get("v")
         if desc.state_bits == 8 and any(getattr(x, "itemsize", 1) != 1 for x in (m, v)):
             raise ValueError("8-bit states are tensors of one byte an element")
