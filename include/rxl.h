@@ -479,8 +479,8 @@ rxl_status rxl_token_logprob_bwd(const rxl_logprob_desc *desc, const void *logit
  *       every step. A
  *       positive r is never rounded to 0.
  *       All states zero (codes and scales) is the state before step 1.
- * A gradient that is not finite spoils its element (8-bit: its block). With
- * eps == 0 an element whose v is 0 divides 0 by 0.
+ * A gradient that is not finite, or so large that v is not, spoils its element
+ * (8-bit: its block). With eps == 0 an element whose v is 0 divides 0 by 0.
  */
 typedef struct {
   void *param;        /* [n] desc.param_dtype, updated in place */

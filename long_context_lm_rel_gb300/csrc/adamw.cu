@@ -2,7 +2,7 @@
 // (include/rxl.h: rxl_adamw_step).
 //
 // Memory-bound: every operand is read once and written once (28 bytes an
-// element for bf16 weights with masters and 32-bit states, 16.25 for f32
+// element for bf16 weights with masters and 32-bit states, 16.13 for f32
 // weights, f32 gradients and 8-bit states). The list travels in the kernel's
 // parameters (up to kPerLaunch tensors a launch, so a 16-layer stack is one
 // launch); a tensor is cut into chunks of 1024 elements, one a block, and a
@@ -17,8 +17,10 @@
 // In 8 bits the 128 elements that share a scale belong to 16 lanes, whose
 // largest magnitudes meet in four shuffles. The exact square root, the exact
 // quotient and the rounding by chance make about a hundred instructions an
-// element, which bounds it: 72 us for 25 M f32 weights, 5.7 TB/s of the 16.25
-// bytes an element, and 595 us for 201 M bf16 ones with masters.
+// element, which bounds it whatever the bytes are: 72 us for 25 M f32 weights
+// (5.6 TB/s of 16.13 bytes an element), 78 for bf16 ones with masters (5.2) and
+// 78 for bf16 alone (3.3 of 10.13); 201 M: 550, 593 and 591 us. At 48 registers
+// each of these kernels stores 48 to 56 bytes a thread to local memory.
 // Sixteen elements a thread: 102 us (registers); 8, 9 or 11 blocks an SM
 // instead of 10: 72 and 634, 70 and 605, 75 and 609; blocks of 256 threads: 74
 // and 612; blocks that take chunks in turn: 2 more.
@@ -78,8 +80,10 @@ __device__ __forceinline__ unsigned dither(unsigned i, unsigned key) {
 // below the kept mantissa, or, below the normal range, to the multiple of the
 // step 2^-9 there. That second case is rare (2^-15 of the block's largest and
 // less, or NaN, which stays) and has a branch of its own for all of them.
-// POSITIVE: what is above 0 stays so. A block's largest, 448 but for two
-// roundings, becomes 448: its last two places and 16 bits carry no further.
+// POSITIVE: what is above 0 stays so. A block's largest is 448 but for two
+// roundings, and becomes 448: above it the last place and 16 bits carry no
+// further; a place or two below it they carry to 448, but for 16 random bits
+// that are all 0 (2^-16: 416, the code below).
 template <bool POSITIVE>
 __device__ __forceinline__ void chance_e4m3(const float (&a)[kPer], const unsigned (&c)[kPer], float (&q)[kPer]) {
   static_assert(kPer == 8);

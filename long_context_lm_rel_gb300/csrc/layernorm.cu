@@ -19,10 +19,10 @@
 // of shared memory, three rows deep, and are read from there for both sweeps.
 //
 // Measured (the card copies at 6.78 TB/s): forward with residual, bf16, 8192 x
-// 1024 12.4 us (5.4 TB/s: five turns of 1824 rows, the last half empty), 32768 x
-// 4096 162 us (6.6), without one 30000 x 4096 78 us (6.3); backward bf16 65536 x
-// 1024 63 us (6.4), 32768 x 4096 135 us (6.0), 8192 x 1024 13.6 us (3.7), f32
-// 5001 x 1023 15.0 us (4.1). What bounds the backward: 7 to 10 us for the first
+// 1024 12.2 us (5.5 TB/s: five turns of 1824 rows, the last half empty), 32768 x
+// 4096 163 us (6.6), without one 30000 x 4096 78 us (6.3); backward bf16 65536 x
+// 1024 62 us (6.5), 32768 x 4096 135 us (6.0), 8192 x 1024 13.4 us (3.8), f32
+// 5001 x 1023 14.9 us (4.1). What bounds the backward: 7 to 10 us for the first
 // rows, the partial sums and the second launch; beyond that 16 warps on an SM
 // (its sums), a row's two sweeps one after the other, within 10% of memory.
 #include <math.h>
@@ -42,9 +42,10 @@ using sm103::griddep_wait;
 // (E 16: 65536 x 1024 bf16 68 us with 512, 77 with 768 and spills; E 8: 20000 x
 // 1024 f32 41 us with 768, 43 with 512; E 32: see by_width_bf16.)
 constexpr int bwd_threads(int E) { return E <= 8 ? 768 : E <= 24 ? 512 : 384; }
-// Rows of a thread in flight or in hand (3, 4, 6: 15.0, 15.2, 16.4 us at 8192 x
-// 1024 bf16; the next row in registers instead: 15.1, but 72 against 68 us at
-// 65536 x 1024).
+// Rows of a thread in flight or in hand (2, 3, 4 and 6, bf16 us: 8192 x 1024
+// 13.4, 13.4, 14.0 and 15.3; 32768 x 4096 141, 135, 136 and 138; 2048 x 4096
+// 16.9, 16.5, 17.2 and 18.8. The next row in registers instead, with 16
+// elements a thread: 72 against 68 us at 65536 x 1024).
 constexpr int kStages = 3;
 
 // A group's place in its block and the E elements its threads hold. VEC:
@@ -502,8 +503,9 @@ norm_bwd_kernel(const T *dy, long long ys, const T *s, long long ss, const T *ga
 }
 
 // Column sums of part [P][2 D] in a fixed order, C columns a block. What
-// bounds it is one wait after the other: with 8 columns a thread has up to 5
-// rows' values, all in flight; with 32 there are fewer blocks to start, which
+// bounds it is one wait after the other: with 8 columns a thread has 5 rows'
+// values in flight, all it has of up to 320 partial rows (of 456, three blocks
+// an SM, it has 8, in two turns); with 32 there are fewer blocks to start, which
 // is better for few rows or wide ones (backward of 8192 x 1024 bf16 with 8 and
 // 32 columns 13.6 and 14.5 us, 2048 x 1024 6.6 and 8.1, 512 x 1024 4.3 and 4.0,
 // 2048 x 8192 27.9 and 26.0).

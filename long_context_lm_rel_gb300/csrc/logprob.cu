@@ -20,11 +20,11 @@
 // block of 64 to 512 threads, or to a cluster of blocks whose results meet in
 // the first one's shared memory (a few very long rows).
 //
-// Measured (the card copies at 6.78 TB/s), bf16: 8192 x 50021 124 us without
+// Measured (the card copies at 6.78 TB/s), bf16: 8192 x 50021 125 us without
 // alternatives (6.6 TB/s) and 147 us with 8 (5.6): the bound costs 6, the list
-// of slots 6, reading them 7, placing the candidates 2, issue slots are 70%
-// busy; 32768 x 8192 85 and 111 us. 65536 x 256 f32 16 and (with 5) 31 us: a
-// row's fixed work is as long as its sum. 4 x 32000 with 20 alternatives 6.5 us.
+// of slots 6, reading them 7, placing the candidates 2, issue slots are 68%
+// busy; 32768 x 8192 83 and 110 us. 65536 x 256 f32 16 and (with 5) 31 us: a
+// row's fixed work is as long as its sum. 4 x 32000 with 20 alternatives 6.3 us.
 //
 // Backward. One pass, a vector in and a vector out: 8192 x 50021 bf16 248 us
 // (6.6 TB/s), 1000 x 10007 f32 13.8 us (5.8).
@@ -973,8 +973,8 @@ constexpr int kThreads = 256;
 constexpr int kGradVectors = 4;  // of a thread
 
 // VEC: input and output rows start at the same place of a vector. A block for
-// each kGradVectors kThreads vectors of a row (twice or half as many: 293 and
-// 309 us, 266 then, at 8192 x 50021). dx may be x.
+// each kGradVectors kThreads vectors of a row (half and twice as many: 274 and
+// 284 us at 8192 x 50021, 247 so). dx may be x.
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(kThreads) logprob_bwd_kernel(const T *x, long long stride, const int32_t *tokens,
                                                                const float *lse, const float *entropy,
