@@ -394,12 +394,14 @@ def _check_adamw_sizes(t):
         need = -(-n // 128) if k.endswith("_scale") else n
         if x.numel() < need:
             raise ValueError(f"{k} has {x.numel()} elements where {need} are read")
+    if n == 0 or all(x.is_contiguous() for x in held.values()):
+        return
     full = [x for k, x in held.items() if not k.endswith("_scale")]
     alike = all(x.shape == full[0].shape and x.stride() == full[0].stride() for x in full)
     for k, x in held.items():
         # without gaps: the last element lies numel - 1 places behind the first
         dense = sum((s - 1) * d for s, d in zip(x.shape, x.stride())) == x.numel() - 1
-        if n > 0 and not x.is_contiguous() and not (alike and dense and not k.endswith("_scale")):
+        if not x.is_contiguous() and not (alike and dense and not k.endswith("_scale")):
             raise ValueError(f"{k} is not contiguous (nor without gaps and in one order with the entry's other tensors)")
 
 
