@@ -288,6 +288,8 @@ norm_fwd_kernel(const T *x, long long xs, const T *res, long long rs, const T *g
     // centres again or that takes D c^2 from the squares: with residual 32768 x
     // 4096 bf16 162, 162, 166, 166; without 65536 x 1024 42.4, 44.6, 43.6, 42.8;
     // 32768 x 4096 85.0, 86.7, 85.7, 88.8; 4500 x 16384 f32 94, 95, 102, 105).
+    // Where all rows are far (mean 100, spread 1): 32768 x 4096 177 and 90 us,
+    // 65536 x 1024 without residual 43.2.
     if constexpr (RES || !AHEAD) {
       float off = mu;
 #pragma unroll 1

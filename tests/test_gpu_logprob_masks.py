@@ -14,7 +14,6 @@ sum and T / S carry it, and lose it again in their difference.
 import pytest
 import torch
 
-import long_context_lm_rel_gb300 as rxl
 from tests.test_gpu_logprob import backward, check_backward, forward, generator
 
 pytestmark = pytest.mark.gpu

@@ -14,7 +14,6 @@ mean. An output is rounded by finfo(t).eps / 2 besides.
 import pytest
 import torch
 
-import long_context_lm_rel_gb300 as rxl
 from tests.test_gpu_norm import forward, generator
 
 pytestmark = pytest.mark.gpu
